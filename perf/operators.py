@@ -23,30 +23,30 @@ def listed():
     return [
         # the queries of one decode step at the benchmark's batch: indexer heads to e4m3 with a scale
         # for each, attention heads rotated in place of their last 64 dims; latency counts
-        dict(name="queries of a decode step 8", op="heads", kind="step", tokens=8, pad=0, dtype="bf16", max_pos=131072),
+        dict(name="queries of a decode step, 8", op="heads", kind="step", tokens=8, pad=0, dtype="bf16", max_pos=131072),
         # the same for the largest batch of the ragged sweep, its last rows padding
-        dict(name="queries of a decode step 256", op="heads", kind="step", tokens=256, pad=13, dtype="bf16", max_pos=16384),
+        dict(name="queries of a decode step, 256", op="heads", kind="step", tokens=256, pad=13, dtype="bf16", max_pos=16384),
         # a prefill chunk: indexer queries and its one key head (layer norm with a bias), both to e4m3
         dict(name="indexer heads of a prefill chunk", op="heads", kind="indexer", tokens=8192, pad=0, dtype="bf16", max_pos=131072),
         # float32 heads of the small configuration, whole head rotated, an odd number of tokens
-        dict(name="float32 heads 4097 tokens", op="heads", kind="plain", tokens=4097, pad=0, dtype="f32", max_pos=8192,
+        dict(name="float32 heads, 4097 tokens", op="heads", kind="plain", tokens=4097, pad=0, dtype="f32", max_pos=8192,
              q_heads=16, k_heads=1, dim=128, rope=128, pairs=False),
         # one new token for each of 8 requests: latent row and indexer key
-        dict(name="append one token 8 requests", op="append", batch=8, new=1, dtype="bf16", max_start=16384, ragged=False),
+        dict(name="append one token, 8 requests", op="append", batch=8, new=1, dtype="bf16", max_start=16384, ragged=False),
         # one new token for each request of the largest sweep batch
-        dict(name="append one token 256 requests", op="append", batch=256, new=1, dtype="bf16", max_start=4096, ragged=False),
+        dict(name="append one token, 256 requests", op="append", batch=256, new=1, dtype="bf16", max_start=4096, ragged=False),
         # a ragged prefill chunk: up to 4096 tokens for each request, some requests with none
         dict(name="append ragged prefill chunk", op="append", batch=16, new=4096, dtype="bf16", max_start=8192, ragged=True),
         # the small float32 configuration: 8 requests, chunks of odd lengths
         dict(name="append float32 rows", op="append", batch=8, new=1000, dtype="f32", max_start=4096, ragged=True),
         # one request with a short context and nothing shared: the smallest call, latency
-        dict(name="attention 1 request of 200", op="prefix", batch=1, heads=128, prefix=0, own_len=200),
+        dict(name="attention, 1 request of 200", op="prefix", batch=1, heads=128, prefix=0, own_len=200),
         # 16 of 128 heads (one rank of eight), many requests behind one system prompt
-        dict(name="attention 64 x 16 heads 8192", op="prefix", batch=64, heads=16, prefix=8192, own_len=512),
+        dict(name="attention, 64 x 16 heads, 8192", op="prefix", batch=64, heads=16, prefix=8192, own_len=512),
         # a ragged batch, prefix of no whole number of pages, own parts of up to 4096 tokens
-        dict(name="attention 16 requests 10007", op="prefix", batch=16, heads=128, prefix=10007, own_len=4096),
+        dict(name="attention, 16 requests, 10007", op="prefix", batch=16, heads=128, prefix=10007, own_len=4096),
         # the benchmark's batch over a shared context of 131072 tokens
-        dict(name="attention 8 requests 131072", op="prefix", batch=8, heads=128, prefix=131072, own_len=1024),
+        dict(name="attention, 8 requests, 131072", op="prefix", batch=8, heads=128, prefix=131072, own_len=1024),
     ]
 
 
