@@ -670,6 +670,7 @@ __global__ void __launch_bounds__(pfx::kThreads, 1)
       ok = softmax_sync_and(good && ok);
       if (!ok) break;
       const float total = (sums[r64] + sums[64 + r64]) + (sums[128 + r64] + sums[192 + r64]);
+      __syncwarp();  // (bar.sync and tcgen05.ld are .aligned: the warp has to be whole before them)
       asm volatile("bar.sync 1, 256;" ::: "memory");
       const float inv = total > 0.f ? 1.f / total : 0.f;
       const int row = w.row0 + rr;
@@ -678,6 +679,7 @@ __global__ void __launch_bounds__(pfx::kThreads, 1)
 #pragma unroll 1
         for (int c0 = cg * 128; c0 < cg * 128 + 128; c0 += 64) {
           float v[64];
+          __syncwarp();  // lanes without a row come here ahead of those that store
           tmem_ld64(tmem + lane_off + c0, v);
           const int d0 = cg * 256 + half * 128 + (c0 & 127);  // column 128 j + c: dim 256 j + 128 half + c
           if (!live) continue;
@@ -724,6 +726,7 @@ __global__ void __launch_bounds__(pfx::kThreads, 1)
           *ml = total > 0.f ? make_float2(m_run, total) : make_float2(-INFINITY, 0.f);
         }
       }
+      __syncwarp();
     }
   }
   __syncwarp();
