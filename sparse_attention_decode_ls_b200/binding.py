@@ -378,18 +378,32 @@ def ls_sparse_attn_decode_noalloc(a: SparseAttnArgs, stream=None):
 
 
 # ------------------------------------------------------------------------------- head rows
+def _require(ok, what):
+    if not ok:
+        raise LsError(LS_ERR_INVALID_ARG, what)
+
+
 def head_rows(x, *, norm=LS_NORM_NONE, norm_dim=None, weight=None, bias=None, eps=1e-6, rope_begin=None,
               rope_layout=LS_ROPE_HALVES) -> HeadRows:
     """One operand of ls_qk_norm_rope (x [tokens, heads, dim]) or ls_cache_append (x [tokens, dim]);
-    x may be a slice of a wider projection (its last stride 1).  norm_dim None: the whole row."""
+    x may be a slice of a wider projection (its last stride 1).  norm_dim None: the whole row.
+    weight / bias [norm_dim], contiguous and of one dtype; either may be absent."""
     shape, stride = x.shape, x.stride()
     dim = shape[-1]
     if stride[-1] != 1 and dim > 1:
         raise LsError(LS_ERR_INVALID_ARG, "the values of a row must be contiguous")
     heads, head_stride = (shape[1], stride[1]) if len(shape) == 3 else (1, 0)
-    r = HeadRows(heads, dim, norm, dim if norm_dim is None else norm_dim, -1 if rope_begin is None else rope_begin,
-                 rope_layout, LS_BF16 if weight is None else _DTYPES[weight.dtype], eps, stride[0], head_stride,
-                 x.data_ptr(), None if weight is None else weight.data_ptr(), None if bias is None else bias.data_ptr())
+    n = dim if norm_dim is None else norm_dim
+    w_dtype, w, b = LS_BF16, None, None
+    if bias is not None:
+        _require(bias.is_contiguous() and bias.numel() >= n, "bias must be contiguous and hold norm_dim values")
+        _require(weight is None or weight.dtype is bias.dtype, "weight and bias must have the same dtype")
+        w_dtype, b = _DTYPES[bias.dtype], bias.data_ptr()
+    if weight is not None:
+        _require(weight.is_contiguous() and weight.numel() >= n, "weight must be contiguous and hold norm_dim values")
+        w_dtype, w = _DTYPES[weight.dtype], weight.data_ptr()
+    r = HeadRows(heads, dim, norm, n, -1 if rope_begin is None else rope_begin, rope_layout, w_dtype, eps, stride[0],
+                 head_stride, x.data_ptr(), w, b)
     r._refs = (x, weight, bias)
     return r
 

@@ -1,0 +1,41 @@
+"""What the Python builders of ls_qk_norm_rope, ls_cache_append and ls_prefix_attn_decode make of their
+tensors, and which they refuse: the library sees addresses only, so types, shapes and strides are
+checked here.  CPU only."""
+import pytest
+import torch
+
+from sparse_attention_decode_ls_b200 import binding as B
+
+BF, F32 = torch.bfloat16, torch.float32
+
+
+# ------------------------------------------------------------------------------- weights and biases
+@pytest.mark.parametrize("weight,bias,want", [
+    (None, None, None), (BF, None, B.LS_BF16), (F32, None, B.LS_F32), (None, BF, B.LS_BF16), (None, F32, B.LS_F32),
+    (BF, BF, B.LS_BF16), (F32, F32, B.LS_F32),
+])
+def test_type_of_weight_and_bias(weight, bias, want):
+    x = torch.zeros(4, 3, 128, dtype=BF)
+    w = None if weight is None else torch.ones(128, dtype=weight)
+    b = None if bias is None else torch.ones(128, dtype=bias)
+    r = B.head_rows(x, norm=B.LS_NORM_LAYER, weight=w, bias=b)
+    if want is not None:
+        assert r.w_dtype == want
+    assert r.weight == (None if w is None else w.data_ptr()) and r.bias == (None if b is None else b.data_ptr())
+
+
+@pytest.mark.parametrize("weight,bias", [
+    (torch.ones(128), torch.ones(128, dtype=BF)), (torch.ones(128, dtype=BF), torch.ones(128)),
+    (torch.ones(127), None), (None, torch.ones(127)), (torch.ones(256)[::2], None), (None, torch.ones(256)[::2]),
+])
+def test_weights_and_biases_that_are_refused(weight, bias):
+    with pytest.raises(B.LsError):
+        B.head_rows(torch.zeros(4, 3, 128, dtype=BF), norm=B.LS_NORM_LAYER, weight=weight, bias=bias)
+
+
+def test_weights_as_long_as_the_normalised_part():
+    x = torch.zeros(4, 576, dtype=BF)
+    r = B.head_rows(x, norm=B.LS_NORM_RMS, norm_dim=512, weight=torch.ones(512))
+    assert (r.norm_dim, r.w_dtype) == (512, B.LS_F32)
+    with pytest.raises(B.LsError):
+        B.head_rows(x, norm=B.LS_NORM_RMS, weight=torch.ones(512))
