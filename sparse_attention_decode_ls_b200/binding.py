@@ -418,12 +418,21 @@ def _head_out(t, scale) -> HeadOut:
 _NO_ROWS = HeadRows()
 
 
+def _rows_alike(x, y, tokens):
+    """The second operand's tensor y beside the first one's: one dtype for both, a row for every token."""
+    _require(x.dtype is y.dtype, "both operands must have the same dtype")
+    _require(x.shape[0] >= tokens and y.shape[0] >= tokens, "an operand has fewer rows than there are tokens")
+
+
 def qk_norm_rope_args(*, pos, cos_sin=None, q=None, q_out=None, q_scale=None, k=None, k_out=None,
                       k_scale=None) -> QkNormRopeArgs:
     """q / k: head_rows operands (or None); q_out / k_out [tokens, heads, dim] of x's dtype, or uint8 /
     float8_e4m3fn with a scale [tokens, heads]; cos_sin [max_pos, rope_dim] float32; pos [tokens] int32."""
     max_pos, rope_dim = (0, 0) if cos_sin is None else cos_sin.shape
-    a = QkNormRopeArgs(pos.shape[0], _DTYPES[(k if q is None else q)._refs[0].dtype], rope_dim, max_pos, pos.data_ptr(),
+    _require(q is not None or k is not None, "neither q nor k is given")
+    x, tokens = (k if q is None else q)._refs[0], pos.shape[0]
+    _rows_alike(x, x if k is None else k._refs[0], tokens)
+    a = QkNormRopeArgs(tokens, _DTYPES[x.dtype], rope_dim, max_pos, pos.data_ptr(),
                        None if cos_sin is None else cos_sin.data_ptr(), _NO_ROWS if q is None else q,
                        _NO_ROWS if k is None else k, _head_out(q_out, q_scale), _head_out(k_out, k_scale))
     a._refs = (q, k, pos, cos_sin, q_out, q_scale, k_out, k_scale)
@@ -440,10 +449,13 @@ def cache_append_args(*, page_table, start, cu_tokens=None, cos_sin=None, kv=Non
                       key_pool=None, key_scale=None) -> CacheAppendArgs:
     """kv / key: head_rows operands of one row per token (or None); kv_pool [num_pages, 64, W] of x's
     dtype; key_pool the same, or uint8 / float8_e4m3fn with key_scale [num_pages, 64]."""
+    _require(kv is not None or key is not None, "neither kv nor key is given")
     x = (key if kv is None else kv)._refs[0]
+    tokens = x.shape[0]
+    _rows_alike(x, x if key is None else key._refs[0], tokens)
     max_pos, rope_dim = (0, 0) if cos_sin is None else cos_sin.shape
     batch, max_pages = page_table.shape
-    a = CacheAppendArgs(batch, x.shape[0], _DTYPES[x.dtype], rope_dim, max_pos, max_pages,
+    a = CacheAppendArgs(batch, tokens, _DTYPES[x.dtype], rope_dim, max_pos, max_pages,
                         0 if key_pool is None else _DTYPES[key_pool.dtype], (key_pool if kv_pool is None else kv_pool).shape[0],
                         0 if kv_pool is None else kv_pool.stride(1), 0 if key_pool is None else key_pool.stride(1),
                         page_table.data_ptr(), start.data_ptr(), _ptr(cu_tokens), _ptr(cos_sin),

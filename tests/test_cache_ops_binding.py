@@ -39,3 +39,47 @@ def test_weights_as_long_as_the_normalised_part():
     assert (r.norm_dim, r.w_dtype) == (512, B.LS_F32)
     with pytest.raises(B.LsError):
         B.head_rows(x, norm=B.LS_NORM_RMS, weight=torch.ones(512))
+
+
+# ------------------------------------------------------------------------------- two operands
+def heads_call(**kw):
+    d = dict(pos=torch.zeros(4, dtype=torch.int32), cos_sin=torch.zeros(100, 64), q=B.head_rows(torch.zeros(4, 3, 128, dtype=BF)),
+             q_out=torch.zeros(4, 3, 128, dtype=BF), k=B.head_rows(torch.zeros(4, 1, 576, dtype=BF)),
+             k_out=torch.zeros(4, 1, 576, dtype=BF))
+    d.update(kw)
+    return B.qk_norm_rope_args(**d)
+
+
+def append_call(**kw):
+    d = dict(page_table=torch.zeros(2, 4, dtype=torch.int32), start=torch.zeros(2, dtype=torch.int32),
+             cu_tokens=torch.tensor([0, 3, 5], dtype=torch.int32), cos_sin=torch.zeros(256, 64),
+             kv=B.head_rows(torch.zeros(5, 576, dtype=BF)), kv_pool=torch.zeros(8, 64, 576, dtype=BF),
+             key=B.head_rows(torch.zeros(5, 128, dtype=BF)), key_pool=torch.zeros(8, 64, 128, dtype=torch.uint8),
+             key_scale=torch.zeros(8, 64))
+    d.update(kw)
+    return B.cache_append_args(**d)
+
+
+def test_operands_of_two_dtypes_are_refused():
+    with pytest.raises(B.LsError):
+        heads_call(k=B.head_rows(torch.zeros(4, 1, 576)))
+    with pytest.raises(B.LsError):
+        append_call(key=B.head_rows(torch.zeros(5, 128)))
+
+
+def test_operands_with_fewer_rows_than_tokens_are_refused():
+    assert heads_call().tokens == 4
+    assert heads_call(pos=torch.zeros(3, dtype=torch.int32)).tokens == 3  # longer buffers are fine
+    for short in (dict(q=B.head_rows(torch.zeros(3, 3, 128, dtype=BF))), dict(k=B.head_rows(torch.zeros(3, 1, 576, dtype=BF)))):
+        with pytest.raises(B.LsError):
+            heads_call(**short)
+    assert append_call().tokens == 5
+    with pytest.raises(B.LsError):
+        append_call(key=B.head_rows(torch.zeros(4, 128, dtype=BF)))
+
+
+def test_a_call_without_operands_is_refused():
+    with pytest.raises(B.LsError):
+        heads_call(q=None, k=None)
+    with pytest.raises(B.LsError):
+        append_call(kv=None, key=None)
