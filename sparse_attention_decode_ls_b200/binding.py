@@ -445,19 +445,38 @@ def ls_qk_norm_rope(*, args=None, stream=None, **tensors):
     _check(lib().ls_qk_norm_rope(C.byref(a), _stream(stream)))
 
 
+def _pool_row_stride(t, width):
+    """The row stride of a pool [num_pages, 64, >= width], which may be a view: the library takes 64 rows
+    of it from page to page."""
+    shape, stride = t.shape, t.stride()
+    _require(len(shape) == 3 and shape[1] == 64 and shape[2] >= width, "a pool is [num_pages, 64, row], its rows no shorter than x's")
+    _require(stride[2] == 1 and (stride[0] == 64 * stride[1] or shape[0] <= 1),
+             "the rows of a pool must be contiguous and its pages 64 row strides apart")
+    return stride[1]
+
+
 def cache_append_args(*, page_table, start, cu_tokens=None, cos_sin=None, kv=None, kv_pool=None, key=None,
                       key_pool=None, key_scale=None) -> CacheAppendArgs:
     """kv / key: head_rows operands of one row per token (or None); kv_pool [num_pages, 64, W] of x's
-    dtype; key_pool the same, or uint8 / float8_e4m3fn with key_scale [num_pages, 64]."""
+    dtype; key_pool the same, or uint8 / float8_e4m3fn with key_scale [num_pages, 64].  A pool may be a
+    view whose pages are 64 row strides apart (a slice of wider rows, a layer of [layers, num_pages, 64, W])."""
     _require(kv is not None or key is not None, "neither kv nor key is given")
     x = (key if kv is None else kv)._refs[0]
     tokens = x.shape[0]
     _rows_alike(x, x if key is None else key._refs[0], tokens)
     max_pos, rope_dim = (0, 0) if cos_sin is None else cos_sin.shape
     batch, max_pages = page_table.shape
+    num_pages, kv_stride, key_stride = 1 << 62, 0, 0
+    if kv is not None:
+        _require(kv_pool is not None and kv_pool.dtype is x.dtype, "kv_pool must be given, in x's dtype")
+        num_pages, kv_stride = kv_pool.shape[0], _pool_row_stride(kv_pool, kv.dim)
+    if key is not None:
+        _require(key_pool is not None, "key_pool must be given")
+        num_pages, key_stride = min(num_pages, key_pool.shape[0]), _pool_row_stride(key_pool, key.dim)
+        _require(key_scale is None or (key_scale.dtype is torch.float32 and key_scale.is_contiguous() and
+                                       key_scale.numel() >= 64 * num_pages), "key_scale must be float32 [num_pages, 64], contiguous")
     a = CacheAppendArgs(batch, tokens, _DTYPES[x.dtype], rope_dim, max_pos, max_pages,
-                        0 if key_pool is None else _DTYPES[key_pool.dtype], (key_pool if kv_pool is None else kv_pool).shape[0],
-                        0 if kv_pool is None else kv_pool.stride(1), 0 if key_pool is None else key_pool.stride(1),
+                        0 if key_pool is None else _DTYPES[key_pool.dtype], num_pages, kv_stride, key_stride,
                         page_table.data_ptr(), start.data_ptr(), _ptr(cu_tokens), _ptr(cos_sin),
                         _NO_ROWS if kv is None else kv, _NO_ROWS if key is None else key,
                         _ptr(kv_pool), _ptr(key_pool), _ptr(key_scale))
@@ -475,8 +494,9 @@ def ls_cache_append(*, args=None, stream=None, **tensors):
 def prefix_attn_args(*, q, kv_pool, page_table, lens, o, lse, scale, prefix_len=0) -> PrefixAttnArgs:
     """q [B,H,576], kv_pool [num_pages,64,W] latent rows, o [B,H,512] bf16 or float32, lse [B,H]."""
     B, H, D = q.shape
+    _require(kv_pool.dtype is q.dtype, "kv_pool must have q's dtype")
     a = PrefixAttnArgs(B, H, D, o.shape[2], _dt(q), _dt(o), page_table.shape[1], int(prefix_len), scale,
-                       kv_pool.shape[0], kv_pool.shape[-1], q.data_ptr(), kv_pool.data_ptr(),
+                       kv_pool.shape[0], _pool_row_stride(kv_pool, D), q.data_ptr(), kv_pool.data_ptr(),
                        page_table.data_ptr(), lens.data_ptr(), o.data_ptr(), lse.data_ptr())
     a._refs = (q, kv_pool, page_table, lens, o, lse)
     return a

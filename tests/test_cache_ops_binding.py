@@ -83,3 +83,51 @@ def test_a_call_without_operands_is_refused():
         heads_call(q=None, k=None)
     with pytest.raises(B.LsError):
         append_call(kv=None, key=None)
+
+
+# ------------------------------------------------------------------------------- pools
+def prefix_call(**kw):
+    d = dict(q=torch.zeros(2, 8, 576, dtype=BF), kv_pool=torch.zeros(8, 64, 576, dtype=BF), page_table=torch.zeros(2, 4, dtype=torch.int32),
+             lens=torch.zeros(2, dtype=torch.int32), o=torch.zeros(2, 8, 512, dtype=BF), lse=torch.zeros(2, 8), scale=1 / 24)
+    d.update(kw)
+    return B.prefix_attn_args(**d)
+
+
+POOL_VIEWS = {
+    "whole": (torch.zeros(8, 64, 576, dtype=BF), 576),
+    "slice of wider rows": (torch.zeros(8, 64, 640, dtype=BF)[:, :, :576], 640),
+    "wider rows": (torch.zeros(8, 64, 640, dtype=BF), 640),
+    "layer of a stack": (torch.zeros(3, 8, 64, 576, dtype=BF)[1], 576),
+    "layer between the rows": (torch.zeros(8, 64, 2, 576, dtype=BF)[:, :, 1], 1152),
+    "one page": (torch.zeros(2, 2, 64, 576, dtype=BF)[:1, 0], 576),
+}
+
+
+@pytest.mark.parametrize("view", POOL_VIEWS)
+def test_append_and_attention_see_the_same_rows_of_a_pool(view):
+    pool, stride = POOL_VIEWS[view]
+    a, p = append_call(kv_pool=pool), prefix_call(kv_pool=pool)
+    assert a.kv_row_stride == p.row_stride == stride
+    assert a.kv_pool == p.kv_pool == pool.data_ptr()
+
+
+@pytest.mark.parametrize("pool", [
+    torch.zeros(8, 2, 64, 576, dtype=BF)[:, 0],              # pages of several layers
+    torch.zeros(8, 32, 576, dtype=BF), torch.zeros(512, 576, dtype=BF), torch.zeros(8, 64, 512, dtype=BF),
+    torch.zeros(8, 64, 1152, dtype=BF)[:, :, ::2], torch.zeros(64, 8, 576, dtype=BF).transpose(0, 1), torch.zeros(8, 64, 576),
+])
+def test_pools_that_are_refused(pool):
+    for call in (append_call, prefix_call):
+        with pytest.raises(B.LsError):
+            call(kv_pool=pool)
+
+
+def test_key_pools():
+    a = append_call(key_pool=torch.zeros(5, 64, 128, dtype=torch.uint8), key_scale=torch.zeros(5, 64))
+    assert a.num_pages == 5 and a.key_row_stride == 128  # a page id has to exist in both pools
+    for bad in (dict(key_pool=torch.zeros(8, 2, 64, 128, dtype=torch.uint8)[:, 0]), dict(key_pool=torch.zeros(8, 64, 64, dtype=torch.uint8)),
+                dict(key_pool=None), dict(kv_pool=None), dict(key_scale=torch.zeros(8, 128)[:, ::2]),
+                dict(key_scale=torch.zeros(7, 64)), dict(key_scale=torch.zeros(8, 64, dtype=BF))):
+        with pytest.raises(B.LsError):
+            append_call(**bad)
+    assert append_call(kv=None, kv_pool=None).kv.heads == 0 and append_call(key=None, key_pool=None, key_scale=None).key.heads == 0

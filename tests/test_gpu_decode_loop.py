@@ -6,6 +6,7 @@ import pytest
 import torch
 
 from sparse_attention_decode_ls_b200 import binding as B
+from test_gpu_prefix_attn import check as check_attention
 
 pytestmark = pytest.mark.gpu
 
@@ -95,4 +96,35 @@ def test_append_query_score_select_attend_in_a_graph():
             assert (l1[b].double() - s.logsumexp(1)).abs().max() <= 1e-4
         # both round P and o to bf16: two roundings each of values below 4
         assert (o1.float() - o2.float()).abs().max() <= 4 * 2.0 ** -7 and (l1 - l2).abs().max() <= 1e-4
+    assert B.ls_check_device_status() == 0
+
+
+@pytest.mark.parametrize("view", ["slice of wider rows", "layer of a stack", "layer between the rows"])
+def test_append_to_a_view_and_attend_over_it(view):
+    """A pool that is a view: the attention reads the rows that the append wrote, and nothing else changes."""
+    g = torch.Generator(device=DEV).manual_seed(2)
+    shape, pick = {"slice of wider rows": ((9, 64, 640), lambda t: t[:, :, :576]),
+                   "layer of a stack": ((3, 9, 64, 576), lambda t: t[1]),
+                   "layer between the rows": ((9, 64, 2, 576), lambda t: t[:, :, 1])}[view]
+    whole = torch.full(shape, 7.0, dtype=torch.bfloat16, device=DEV)
+    pool = pick(whole)
+    table = torch.randperm(9, generator=g, device=DEV)[:8].to(torch.int32).view(2, 4)
+    x = torch.randn(300, 576, generator=g, device=DEV).to(torch.bfloat16)
+    lens = [130, 170]
+    B.ls_cache_append(page_table=table, start=torch.zeros(2, dtype=torch.int32, device=DEV),
+                      cu_tokens=torch.tensor([0, 130, 300], dtype=torch.int32, device=DEV), kv=B.head_rows(x), kv_pool=pool)
+    q = torch.randn(2, 16, 576, generator=g, device=DEV).to(torch.bfloat16)
+    o, lse = torch.zeros(2, 16, 512, dtype=torch.bfloat16, device=DEV), torch.zeros(2, 16, device=DEV)
+    a = B.prefix_attn_args(q=q, kv_pool=pool, page_table=table, lens=torch.tensor(lens, dtype=torch.int32, device=DEV), o=o, lse=lse,
+                           scale=SCALE)
+    B.ls_prefix_attn_decode(a, torch.empty(max(256, B.ls_prefix_attn_workspace_size(a)), dtype=torch.uint8, device=DEV))
+    want = torch.full(shape, 7.0, dtype=torch.bfloat16, device=DEV)
+    at = 0
+    for b, n in enumerate(lens):
+        rows = x[at: at + n]
+        pos = torch.arange(n, device=DEV)
+        pick(want)[table[b, pos // 64].long(), pos % 64] = rows
+        at += n
+    assert torch.equal(whole, want)
+    check_attention(dict(q=q, pool=pick(want), table=table), o, lse, scale=SCALE, lens=lens)
     assert B.ls_check_device_status() == 0
