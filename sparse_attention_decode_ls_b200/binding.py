@@ -408,6 +408,21 @@ def head_rows(x, *, norm=LS_NORM_NONE, norm_dim=None, weight=None, bias=None, ep
     return r
 
 
+def _ints(t, n, what):
+    """Positions, lengths, page ids: int32, as the library reads them (torch makes int64 by default)."""
+    if t.dtype is not torch.int32 or not t.is_contiguous() or t.numel() < n:
+        raise LsError(LS_ERR_INVALID_ARG, what + " must be int32, contiguous and long enough")
+    return t.data_ptr()
+
+
+def _angle_table(t):
+    if t is None:
+        return 0, 0, None
+    _require(t.dtype is torch.float32 and t.is_contiguous() and t.dim() == 2, "cos_sin must be float32 [max_pos, rope_dim], contiguous")
+    max_pos, rope_dim = t.shape
+    return max_pos, rope_dim, t.data_ptr()
+
+
 def _head_out(t, scale) -> HeadOut:
     if t is None:
         return HeadOut()
@@ -428,13 +443,12 @@ def qk_norm_rope_args(*, pos, cos_sin=None, q=None, q_out=None, q_scale=None, k=
                       k_scale=None) -> QkNormRopeArgs:
     """q / k: head_rows operands (or None); q_out / k_out [tokens, heads, dim] of x's dtype, or uint8 /
     float8_e4m3fn with a scale [tokens, heads]; cos_sin [max_pos, rope_dim] float32; pos [tokens] int32."""
-    max_pos, rope_dim = (0, 0) if cos_sin is None else cos_sin.shape
+    max_pos, rope_dim, angles = _angle_table(cos_sin)
     _require(q is not None or k is not None, "neither q nor k is given")
     x, tokens = (k if q is None else q)._refs[0], pos.shape[0]
     _rows_alike(x, x if k is None else k._refs[0], tokens)
-    a = QkNormRopeArgs(tokens, _DTYPES[x.dtype], rope_dim, max_pos, pos.data_ptr(),
-                       None if cos_sin is None else cos_sin.data_ptr(), _NO_ROWS if q is None else q,
-                       _NO_ROWS if k is None else k, _head_out(q_out, q_scale), _head_out(k_out, k_scale))
+    a = QkNormRopeArgs(tokens, _DTYPES[x.dtype], rope_dim, max_pos, _ints(pos, tokens, "pos"), angles,
+                       _NO_ROWS if q is None else q, _NO_ROWS if k is None else k, _head_out(q_out, q_scale), _head_out(k_out, k_scale))
     a._refs = (q, k, pos, cos_sin, q_out, q_scale, k_out, k_scale)
     return a
 
@@ -464,7 +478,7 @@ def cache_append_args(*, page_table, start, cu_tokens=None, cos_sin=None, kv=Non
     x = (key if kv is None else kv)._refs[0]
     tokens = x.shape[0]
     _rows_alike(x, x if key is None else key._refs[0], tokens)
-    max_pos, rope_dim = (0, 0) if cos_sin is None else cos_sin.shape
+    max_pos, rope_dim, angles = _angle_table(cos_sin)
     batch, max_pages = page_table.shape
     num_pages, kv_stride, key_stride = 1 << 62, 0, 0
     if kv is not None:
@@ -477,7 +491,8 @@ def cache_append_args(*, page_table, start, cu_tokens=None, cos_sin=None, kv=Non
                                        key_scale.numel() >= 64 * num_pages), "key_scale must be float32 [num_pages, 64], contiguous")
     a = CacheAppendArgs(batch, tokens, _DTYPES[x.dtype], rope_dim, max_pos, max_pages,
                         0 if key_pool is None else _DTYPES[key_pool.dtype], num_pages, kv_stride, key_stride,
-                        page_table.data_ptr(), start.data_ptr(), _ptr(cu_tokens), _ptr(cos_sin),
+                        _ints(page_table, 0, "page_table"), _ints(start, batch, "start"),
+                        None if cu_tokens is None else _ints(cu_tokens, batch + 1, "cu_tokens"), angles,
                         _NO_ROWS if kv is None else kv, _NO_ROWS if key is None else key,
                         _ptr(kv_pool), _ptr(key_pool), _ptr(key_scale))
     a._refs = (kv, key, page_table, start, cu_tokens, cos_sin, kv_pool, key_pool, key_scale)
@@ -497,7 +512,8 @@ def prefix_attn_args(*, q, kv_pool, page_table, lens, o, lse, scale, prefix_len=
     _require(kv_pool.dtype is q.dtype, "kv_pool must have q's dtype")
     a = PrefixAttnArgs(B, H, D, o.shape[2], _dt(q), _dt(o), page_table.shape[1], int(prefix_len), scale,
                        kv_pool.shape[0], _pool_row_stride(kv_pool, D), q.data_ptr(), kv_pool.data_ptr(),
-                       page_table.data_ptr(), lens.data_ptr(), o.data_ptr(), lse.data_ptr())
+                       _ints(page_table, B * page_table.shape[1], "page_table"), _ints(lens, B, "lens"), o.data_ptr(),
+                       lse.data_ptr())
     a._refs = (q, kv_pool, page_table, lens, o, lse)
     return a
 

@@ -131,3 +131,46 @@ def test_key_pools():
         with pytest.raises(B.LsError):
             append_call(**bad)
     assert append_call(kv=None, kv_pool=None).kv.heads == 0 and append_call(key=None, key_pool=None, key_scale=None).key.heads == 0
+
+
+# ------------------------------------------------------------------------------- positions, lengths, tables
+I64 = torch.int64
+
+
+@pytest.mark.parametrize("pos", [torch.zeros(4, dtype=I64), torch.zeros(4), torch.zeros(8, dtype=torch.int32)[::2]])
+def test_positions_are_int32_and_contiguous(pos):
+    with pytest.raises(B.LsError):
+        heads_call(pos=pos)
+
+
+@pytest.mark.parametrize("cos_sin", [torch.zeros(100, 64, dtype=torch.float64), torch.zeros(100, 64, dtype=BF), torch.zeros(100, 128)[:, :64],
+                                     torch.zeros(100, 32, 2)])
+def test_angle_tables_that_are_refused(cos_sin):
+    for call in (heads_call, append_call):
+        with pytest.raises(B.LsError):
+            call(cos_sin=cos_sin)
+
+
+def test_angle_table_as_given():
+    t = torch.zeros(100, 64)
+    for a in (heads_call(cos_sin=t), append_call(cos_sin=t)):
+        assert (a.max_pos, a.rope_dim, a.cos_sin) == (100, 64, t.data_ptr())
+
+
+@pytest.mark.parametrize("kw", [
+    dict(start=torch.zeros(2, dtype=I64)), dict(start=torch.zeros(1, dtype=torch.int32)), dict(start=torch.zeros(4, dtype=torch.int32)[::2]),
+    dict(cu_tokens=torch.tensor([0, 3, 5])), dict(cu_tokens=torch.tensor([0, 3], dtype=torch.int32)),
+    dict(page_table=torch.zeros(2, 4, dtype=I64)), dict(page_table=torch.zeros(2, 8, dtype=torch.int32)[:, :4]),
+])
+def test_append_indices_that_are_refused(kw):
+    with pytest.raises(B.LsError):
+        append_call(**kw)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(lens=torch.zeros(2, dtype=I64)), dict(lens=torch.zeros(1, dtype=torch.int32)), dict(page_table=torch.zeros(2, 4, dtype=I64)),
+    dict(page_table=torch.zeros(2, 8, dtype=torch.int32)[:, :4]), dict(page_table=torch.zeros(1, 4, dtype=torch.int32)),
+])
+def test_attention_indices_that_are_refused(kw):
+    with pytest.raises(B.LsError):
+        prefix_call(**kw)
