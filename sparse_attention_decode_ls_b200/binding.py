@@ -423,14 +423,25 @@ def _angle_table(t):
     return max_pos, rope_dim, t.data_ptr()
 
 
-def _head_out(t, scale) -> HeadOut:
-    if t is None:
-        return HeadOut()
-    stride = t.stride()
-    return HeadOut(_DTYPES[t.dtype], stride[0], stride[1], t.data_ptr(), None if scale is None else scale.data_ptr())
+_NO_ROWS, _NO_OUT = HeadRows(), HeadOut()
 
 
-_NO_ROWS = HeadRows()
+def _head_out(r, t, scale, tokens) -> HeadOut:
+    """t [>= tokens, heads, dim] (or [>= tokens, dim] for one head), any strides but the last's."""
+    if r is None:
+        return _NO_OUT
+    _require(t is not None, "an operand has no output")
+    shape, stride, heads, dim = t.shape, t.stride(), r.heads, r.dim
+    _require(shape[0] >= tokens and shape[-1] == dim and (len(shape) == 3 and shape[1] == heads or len(shape) == 2 and heads == 1),
+             "an output must be [tokens, heads, dim]")
+    _require(stride[-1] == 1 or dim == 1, "the values of an output row must be contiguous")
+    if scale is None:
+        s = None
+    else:
+        _require(scale.dtype is torch.float32 and scale.is_contiguous() and scale.numel() >= tokens * heads,
+                 "a scale must be float32 [tokens, heads], contiguous")
+        s = scale.data_ptr()
+    return HeadOut(_DTYPES[t.dtype], stride[0], stride[1], t.data_ptr(), s)
 
 
 def _rows_alike(x, y, tokens):
@@ -448,7 +459,8 @@ def qk_norm_rope_args(*, pos, cos_sin=None, q=None, q_out=None, q_scale=None, k=
     x, tokens = (k if q is None else q)._refs[0], pos.shape[0]
     _rows_alike(x, x if k is None else k._refs[0], tokens)
     a = QkNormRopeArgs(tokens, _DTYPES[x.dtype], rope_dim, max_pos, _ints(pos, tokens, "pos"), angles,
-                       _NO_ROWS if q is None else q, _NO_ROWS if k is None else k, _head_out(q_out, q_scale), _head_out(k_out, k_scale))
+                       _NO_ROWS if q is None else q, _NO_ROWS if k is None else k, _head_out(q, q_out, q_scale, tokens),
+                       _head_out(k, k_out, k_scale, tokens))
     a._refs = (q, k, pos, cos_sin, q_out, q_scale, k_out, k_scale)
     return a
 
@@ -510,6 +522,8 @@ def prefix_attn_args(*, q, kv_pool, page_table, lens, o, lse, scale, prefix_len=
     """q [B,H,576], kv_pool [num_pages,64,W] latent rows, o [B,H,512] bf16 or float32, lse [B,H]."""
     B, H, D = q.shape
     _require(kv_pool.dtype is q.dtype, "kv_pool must have q's dtype")
+    _require(q.is_contiguous() and o.is_contiguous() and o.shape[0] >= B and o.shape[1] == H, "q and o must be contiguous, o [B, H, dv]")
+    _require(lse.dtype is torch.float32 and lse.is_contiguous() and lse.numel() >= B * H, "lse must be float32 [B, H], contiguous")
     a = PrefixAttnArgs(B, H, D, o.shape[2], _dt(q), _dt(o), page_table.shape[1], int(prefix_len), scale,
                        kv_pool.shape[0], _pool_row_stride(kv_pool, D), q.data_ptr(), kv_pool.data_ptr(),
                        _ints(page_table, B * page_table.shape[1], "page_table"), _ints(lens, B, "lens"), o.data_ptr(),

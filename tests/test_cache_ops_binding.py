@@ -174,3 +174,42 @@ def test_append_indices_that_are_refused(kw):
 def test_attention_indices_that_are_refused(kw):
     with pytest.raises(B.LsError):
         prefix_call(**kw)
+
+
+# ------------------------------------------------------------------------------- outputs
+U8 = torch.uint8
+
+
+@pytest.mark.parametrize("kw", [
+    dict(q_out=None), dict(q_out=torch.zeros(3, 3, 128, dtype=BF)), dict(q_out=torch.zeros(4, 2, 128, dtype=BF)),
+    dict(q_out=torch.zeros(4, 3, 64, dtype=BF)), dict(q_out=torch.zeros(4, 128, dtype=BF)), dict(q_out=torch.zeros(4, 3, 256, dtype=BF)[:, :, ::2]),
+    dict(k_out=torch.zeros(3, 1, 576, dtype=BF)), dict(k_out=torch.zeros(4, 2, 576, dtype=BF)),
+    dict(q_out=torch.zeros(4, 3, 128, dtype=U8), q_scale=torch.zeros(4, 6)[:, ::2]),
+    dict(q_out=torch.zeros(4, 3, 128, dtype=U8), q_scale=torch.zeros(4, 2)),
+    dict(q_out=torch.zeros(4, 3, 128, dtype=U8), q_scale=torch.zeros(4, 3, dtype=BF)),
+])
+def test_outputs_of_head_rows_that_are_refused(kw):
+    with pytest.raises(B.LsError):
+        heads_call(**kw)
+
+
+def test_outputs_of_head_rows_as_given():
+    t = torch.zeros(3, 9, 128, dtype=U8)
+    sc = torch.zeros(9, 3)
+    a = heads_call(q_out=t.transpose(0, 1), q_scale=sc)
+    assert (a.q_out.token_stride, a.q_out.head_stride, a.q_out.dtype) == (128, 9 * 128, B.LS_E4M3)
+    assert (a.q_out.out, a.q_out.scale) == (t.data_ptr(), sc.data_ptr())
+    a = heads_call(k=B.head_rows(torch.zeros(4, 576, dtype=BF)), k_out=torch.zeros(4, 640, dtype=BF)[:, :576])
+    assert a.k_out.token_stride == 640 and a.k.heads == 1
+    a = heads_call(k=None, k_out=None)
+    assert a.k.heads == 0 and a.k_out.out is None
+
+
+@pytest.mark.parametrize("kw", [
+    dict(q=torch.zeros(2, 8, 640, dtype=BF)[:, :, :576]), dict(o=torch.zeros(1, 8, 512, dtype=BF)), dict(o=torch.zeros(2, 4, 512, dtype=BF)),
+    dict(o=torch.zeros(2, 8, 1024, dtype=BF)[:, :, :512]), dict(lse=torch.zeros(2, 7)), dict(lse=torch.zeros(2, 16)[:, ::2]),
+    dict(lse=torch.zeros(2, 8, dtype=BF)),
+])
+def test_queries_and_outputs_of_the_attention_that_are_refused(kw):
+    with pytest.raises(B.LsError):
+        prefix_call(**kw)
