@@ -93,11 +93,13 @@ class HeadOut(C.Structure):
 
 
 class QkNormRopeArgs(C.Structure):
+    _refs, _device = (), None  # (see _check_device)
     _fields_ = [("tokens", _i32), ("dtype", _i32), ("rope_dim", _i32), ("max_pos", _i32), ("pos", _p),
                 ("cos_sin", _p), ("q", HeadRows), ("k", HeadRows), ("q_out", HeadOut), ("k_out", HeadOut)]
 
 
 class CacheAppendArgs(C.Structure):
+    _refs, _device = (), None  # (see _check_device)
     _fields_ = [("batch", _i32), ("tokens", _i32), ("dtype", _i32), ("rope_dim", _i32), ("max_pos", _i32),
                 ("max_pages", _i32), ("key_dtype", _i32), ("num_pages", _i64), ("kv_row_stride", _i64),
                 ("key_row_stride", _i64), ("page_table", _p), ("start", _p), ("cu_tokens", _p), ("cos_sin", _p),
@@ -105,6 +107,7 @@ class CacheAppendArgs(C.Structure):
 
 
 class PrefixAttnArgs(C.Structure):
+    _refs, _device = (), None  # (see _check_device)
     _fields_ = [("batch", _i32), ("heads", _i32), ("dk", _i32), ("dv", _i32), ("dtype", _i32), ("o_dtype", _i32),
                 ("max_pages", _i32), ("prefix_len", _i32), ("softmax_scale", _f32), ("num_pages", _i64),
                 ("row_stride", _i64), ("q", _p), ("kv_pool", _p), ("page_table", _p), ("lens", _p), ("o", _p),
@@ -222,10 +225,10 @@ def _hold(a, *objs):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _stream(stream):
+def _stream(stream, device=None):
     if stream is None:
         if _raw_stream is not None:
-            return _raw_stream(torch.cuda.current_device())
+            return _raw_stream(torch.cuda.current_device() if device is None else device)
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
@@ -378,11 +381,6 @@ def ls_sparse_attn_decode_noalloc(a: SparseAttnArgs, stream=None):
 
 
 # ------------------------------------------------------------------------------- head rows
-def _require(ok, what):
-    if not ok:
-        raise LsError(LS_ERR_INVALID_ARG, what)
-
-
 def head_rows(x, *, norm=LS_NORM_NONE, norm_dim=None, weight=None, bias=None, eps=1e-6, rope_begin=None,
               rope_layout=LS_ROPE_HALVES) -> HeadRows:
     """One operand of ls_qk_norm_rope (x [tokens, heads, dim]) or ls_cache_append (x [tokens, dim]);
@@ -396,16 +394,27 @@ def head_rows(x, *, norm=LS_NORM_NONE, norm_dim=None, weight=None, bias=None, ep
     n = dim if norm_dim is None else norm_dim
     w_dtype, w, b = LS_BF16, None, None
     if bias is not None:
-        _require(bias.is_contiguous() and bias.numel() >= n, "bias must be contiguous and hold norm_dim values")
-        _require(weight is None or weight.dtype is bias.dtype, "weight and bias must have the same dtype")
+        if not bias.is_contiguous() or bias.numel() < n or (weight is not None and weight.dtype is not bias.dtype):
+            raise LsError(LS_ERR_INVALID_ARG, "bias must be contiguous, hold norm_dim values and have the weight's dtype")
         w_dtype, b = _DTYPES[bias.dtype], bias.data_ptr()
     if weight is not None:
-        _require(weight.is_contiguous() and weight.numel() >= n, "weight must be contiguous and hold norm_dim values")
+        if not weight.is_contiguous() or weight.numel() < n:
+            raise LsError(LS_ERR_INVALID_ARG, "weight must be contiguous and hold norm_dim values")
         w_dtype, w = _DTYPES[weight.dtype], weight.data_ptr()
     r = HeadRows(heads, dim, norm, n, -1 if rope_begin is None else rope_begin, rope_layout, w_dtype, eps, stride[0],
                  head_stride, x.data_ptr(), w, b)
     r._refs = (x, weight, bias)
+    r._like = shape, x.dtype
     return r
+
+
+def _check_device(a, device):
+    """Every tensor of a call lies on the current device, where the kernel runs, or in pinned host
+    memory; looked at once per argument struct and device."""
+    for t in a._refs:
+        if t is not None and t.get_device() != device and not (t.get_device() < 0 and t.is_pinned()):
+            raise LsError(LS_ERR_INVALID_ARG, "a tensor is neither on the current device nor in pinned host memory")
+    a._device = device
 
 
 def _ints(t, n, what):
@@ -418,9 +427,10 @@ def _ints(t, n, what):
 def _angle_table(t):
     if t is None:
         return 0, 0, None
-    _require(t.dtype is torch.float32 and t.is_contiguous() and t.dim() == 2, "cos_sin must be float32 [max_pos, rope_dim], contiguous")
-    max_pos, rope_dim = t.shape
-    return max_pos, rope_dim, t.data_ptr()
+    shape = t.shape
+    if t.dtype is not torch.float32 or not t.is_contiguous() or len(shape) != 2:
+        raise LsError(LS_ERR_INVALID_ARG, "cos_sin must be float32 [max_pos, rope_dim], contiguous")
+    return shape[0], shape[1], t.data_ptr()
 
 
 _NO_ROWS, _NO_OUT = HeadRows(), HeadOut()
@@ -428,26 +438,36 @@ _NO_ROWS, _NO_OUT = HeadRows(), HeadOut()
 
 def _head_out(r, t, scale, tokens) -> HeadOut:
     """t [>= tokens, heads, dim] (or [>= tokens, dim] for one head), any strides but the last's."""
-    if r is None:
-        return _NO_OUT
-    _require(t is not None, "an operand has no output")
-    shape, stride, heads, dim = t.shape, t.stride(), r.heads, r.dim
-    _require(shape[0] >= tokens and shape[-1] == dim and (len(shape) == 3 and shape[1] == heads or len(shape) == 2 and heads == 1),
-             "an output must be [tokens, heads, dim]")
-    _require(stride[-1] == 1 or dim == 1, "the values of an output row must be contiguous")
+    if t is None:
+        raise LsError(LS_ERR_INVALID_ARG, "an operand has no output")
+    shape, stride = t.shape, t.stride()
+    if shape != r._like[0] and (shape[0] < tokens or shape[-1] != r.dim or
+                                not (len(shape) == 2 and r.heads == 1 or len(shape) == 3 and shape[1] == r.heads)):
+        raise LsError(LS_ERR_INVALID_ARG, "an output must be [tokens, heads, dim]")
+    if stride[-1] != 1 and shape[-1] > 1:
+        raise LsError(LS_ERR_INVALID_ARG, "the values of an output row must be contiguous")
     if scale is None:
-        s = None
-    else:
-        _require(scale.dtype is torch.float32 and scale.is_contiguous() and scale.numel() >= tokens * heads,
-                 "a scale must be float32 [tokens, heads], contiguous")
-        s = scale.data_ptr()
-    return HeadOut(_DTYPES[t.dtype], stride[0], stride[1], t.data_ptr(), s)
+        return HeadOut(_DTYPES[t.dtype], stride[0], stride[1], t.data_ptr())
+    if scale.dtype is not torch.float32 or not scale.is_contiguous() or scale.numel() < tokens * r.heads:
+        raise LsError(LS_ERR_INVALID_ARG, "a scale must be float32 [tokens, heads], contiguous")
+    return HeadOut(_DTYPES[t.dtype], stride[0], stride[1], t.data_ptr(), scale.data_ptr())
 
 
-def _rows_alike(x, y, tokens):
-    """The second operand's tensor y beside the first one's: one dtype for both, a row for every token."""
-    _require(x.dtype is y.dtype, "both operands must have the same dtype")
-    _require(x.shape[0] >= tokens and y.shape[0] >= tokens, "an operand has fewer rows than there are tokens")
+def _operands(r, s, tokens):
+    """Both operands (either may be absent, not both) have one dtype and a row for every token (None: as
+    many as the first one has).  The first one that is given, and the tokens."""
+    if r is None:
+        r = s
+        if r is None:
+            raise LsError(LS_ERR_INVALID_ARG, "neither operand is given")
+    shape, dtype = r._like
+    if tokens is None:
+        tokens = shape[0]
+    if shape[0] < tokens:
+        raise LsError(LS_ERR_INVALID_ARG, "an operand has fewer rows than there are tokens")
+    if s is not None and (s._like[1] is not dtype or s._like[0][0] < tokens):
+        raise LsError(LS_ERR_INVALID_ARG, "the second operand has another dtype than the first or too few rows")
+    return r, dtype, tokens
 
 
 def qk_norm_rope_args(*, pos, cos_sin=None, q=None, q_out=None, q_scale=None, k=None, k_out=None,
@@ -455,30 +475,33 @@ def qk_norm_rope_args(*, pos, cos_sin=None, q=None, q_out=None, q_scale=None, k=
     """q / k: head_rows operands (or None); q_out / k_out [tokens, heads, dim] of x's dtype, or uint8 /
     float8_e4m3fn with a scale [tokens, heads]; cos_sin [max_pos, rope_dim] float32; pos [tokens] int32."""
     max_pos, rope_dim, angles = _angle_table(cos_sin)
-    _require(q is not None or k is not None, "neither q nor k is given")
-    x, tokens = (k if q is None else q)._refs[0], pos.shape[0]
-    _rows_alike(x, x if k is None else k._refs[0], tokens)
-    a = QkNormRopeArgs(tokens, _DTYPES[x.dtype], rope_dim, max_pos, _ints(pos, tokens, "pos"), angles,
-                       _NO_ROWS if q is None else q, _NO_ROWS if k is None else k, _head_out(q, q_out, q_scale, tokens),
-                       _head_out(k, k_out, k_scale, tokens))
-    a._refs = (q, k, pos, cos_sin, q_out, q_scale, k_out, k_scale)
+    r, dtype, tokens = _operands(q, k, pos.numel())
+    a = QkNormRopeArgs(tokens, _DTYPES[dtype], rope_dim, max_pos, _ints(pos, tokens, "pos"), angles,
+                       _NO_ROWS if q is None else q, _NO_ROWS if k is None else k,
+                       _NO_OUT if q is None else _head_out(q, q_out, q_scale, tokens),
+                       _NO_OUT if k is None else _head_out(k, k_out, k_scale, tokens))
+    a._refs = r._refs + (pos, cos_sin, q_out, q_scale, k_out, k_scale) + (() if k is None or k is r else k._refs)
     return a
 
 
 def ls_qk_norm_rope(*, args=None, stream=None, **tensors):
     """qk_norm_rope_args' tensors, or `args` built from them before."""
     a = qk_norm_rope_args(**tensors) if args is None else args
-    _check(lib().ls_qk_norm_rope(C.byref(a), _stream(stream)))
+    device = torch.cuda.current_device()
+    if a._device != device:
+        _check_device(a, device)
+    _check(lib().ls_qk_norm_rope(C.byref(a), _stream(stream, device)))
 
 
-def _pool_row_stride(t, width):
-    """The row stride of a pool [num_pages, 64, >= width], which may be a view: the library takes 64 rows
-    of it from page to page."""
+def _pool(t, width):
+    """Pages and row stride of a pool [num_pages, 64, >= width], which may be a view: the library takes
+    64 rows of it from page to page."""
     shape, stride = t.shape, t.stride()
-    _require(len(shape) == 3 and shape[1] == 64 and shape[2] >= width, "a pool is [num_pages, 64, row], its rows no shorter than x's")
-    _require(stride[2] == 1 and (stride[0] == 64 * stride[1] or shape[0] <= 1),
-             "the rows of a pool must be contiguous and its pages 64 row strides apart")
-    return stride[1]
+    if len(shape) != 3 or shape[1] != 64 or shape[2] < width:
+        raise LsError(LS_ERR_INVALID_ARG, "a pool is [num_pages, 64, row], its rows no shorter than x's")
+    if stride[2] != 1 or (stride[0] != 64 * stride[1] and shape[0] > 1):
+        raise LsError(LS_ERR_INVALID_ARG, "the rows of a pool must be contiguous and its pages 64 row strides apart")
+    return shape[0], stride[1]
 
 
 def cache_append_args(*, page_table, start, cu_tokens=None, cos_sin=None, kv=None, kv_pool=None, key=None,
@@ -486,48 +509,58 @@ def cache_append_args(*, page_table, start, cu_tokens=None, cos_sin=None, kv=Non
     """kv / key: head_rows operands of one row per token (or None); kv_pool [num_pages, 64, W] of x's
     dtype; key_pool the same, or uint8 / float8_e4m3fn with key_scale [num_pages, 64].  A pool may be a
     view whose pages are 64 row strides apart (a slice of wider rows, a layer of [layers, num_pages, 64, W])."""
-    _require(kv is not None or key is not None, "neither kv nor key is given")
-    x = (key if kv is None else kv)._refs[0]
-    tokens = x.shape[0]
-    _rows_alike(x, x if key is None else key._refs[0], tokens)
+    r, dtype, tokens = _operands(kv, key, None)
     max_pos, rope_dim, angles = _angle_table(cos_sin)
     batch, max_pages = page_table.shape
     num_pages, kv_stride, key_stride = 1 << 62, 0, 0
     if kv is not None:
-        _require(kv_pool is not None and kv_pool.dtype is x.dtype, "kv_pool must be given, in x's dtype")
-        num_pages, kv_stride = kv_pool.shape[0], _pool_row_stride(kv_pool, kv.dim)
+        if kv_pool is None or kv_pool.dtype is not dtype:
+            raise LsError(LS_ERR_INVALID_ARG, "kv_pool must be given, in x's dtype")
+        num_pages, kv_stride = _pool(kv_pool, kv.dim)
     if key is not None:
-        _require(key_pool is not None, "key_pool must be given")
-        num_pages, key_stride = min(num_pages, key_pool.shape[0]), _pool_row_stride(key_pool, key.dim)
-        _require(key_scale is None or (key_scale.dtype is torch.float32 and key_scale.is_contiguous() and
-                                       key_scale.numel() >= 64 * num_pages), "key_scale must be float32 [num_pages, 64], contiguous")
-    a = CacheAppendArgs(batch, tokens, _DTYPES[x.dtype], rope_dim, max_pos, max_pages,
+        if key_pool is None:
+            raise LsError(LS_ERR_INVALID_ARG, "key_pool must be given")
+        n, key_stride = _pool(key_pool, key.dim)
+        num_pages = min(num_pages, n)
+        if key_scale is not None and (key_scale.dtype is not torch.float32 or not key_scale.is_contiguous() or
+                                      key_scale.numel() < 64 * num_pages):
+            raise LsError(LS_ERR_INVALID_ARG, "key_scale must be float32 [num_pages, 64], contiguous")
+    a = CacheAppendArgs(batch, tokens, _DTYPES[dtype], rope_dim, max_pos, max_pages,
                         0 if key_pool is None else _DTYPES[key_pool.dtype], num_pages, kv_stride, key_stride,
                         _ints(page_table, 0, "page_table"), _ints(start, batch, "start"),
                         None if cu_tokens is None else _ints(cu_tokens, batch + 1, "cu_tokens"), angles,
                         _NO_ROWS if kv is None else kv, _NO_ROWS if key is None else key,
                         _ptr(kv_pool), _ptr(key_pool), _ptr(key_scale))
-    a._refs = (kv, key, page_table, start, cu_tokens, cos_sin, kv_pool, key_pool, key_scale)
+    a._refs = r._refs + (page_table, start, cu_tokens, cos_sin, kv_pool, key_pool, key_scale) + (
+        () if key is None or key is r else key._refs)
     return a
 
 
 def ls_cache_append(*, args=None, stream=None, **tensors):
     """cache_append_args' tensors, or `args` built from them before."""
     a = cache_append_args(**tensors) if args is None else args
-    _check(lib().ls_cache_append(C.byref(a), _stream(stream)))
+    device = torch.cuda.current_device()
+    if a._device != device:
+        _check_device(a, device)
+    _check(lib().ls_cache_append(C.byref(a), _stream(stream, device)))
 
 
 # ------------------------------------------------------------------------------- shared prefix
 def prefix_attn_args(*, q, kv_pool, page_table, lens, o, lse, scale, prefix_len=0) -> PrefixAttnArgs:
     """q [B,H,576], kv_pool [num_pages,64,W] latent rows, o [B,H,512] bf16 or float32, lse [B,H]."""
     B, H, D = q.shape
-    _require(kv_pool.dtype is q.dtype, "kv_pool must have q's dtype")
-    _require(q.is_contiguous() and o.is_contiguous() and o.shape[0] >= B and o.shape[1] == H, "q and o must be contiguous, o [B, H, dv]")
-    _require(lse.dtype is torch.float32 and lse.is_contiguous() and lse.numel() >= B * H, "lse must be float32 [B, H], contiguous")
-    a = PrefixAttnArgs(B, H, D, o.shape[2], _dt(q), _dt(o), page_table.shape[1], int(prefix_len), scale,
-                       kv_pool.shape[0], _pool_row_stride(kv_pool, D), q.data_ptr(), kv_pool.data_ptr(),
-                       _ints(page_table, B * page_table.shape[1], "page_table"), _ints(lens, B, "lens"), o.data_ptr(),
-                       lse.data_ptr())
+    rows, heads, dv = o.shape
+    dtype = q.dtype
+    if kv_pool.dtype is not dtype:
+        raise LsError(LS_ERR_INVALID_ARG, "kv_pool must have q's dtype")
+    if not q.is_contiguous() or not o.is_contiguous() or rows < B or heads != H:
+        raise LsError(LS_ERR_INVALID_ARG, "q and o must be contiguous, o [B, H, dv]")
+    if lse.dtype is not torch.float32 or not lse.is_contiguous() or lse.numel() < B * H:
+        raise LsError(LS_ERR_INVALID_ARG, "lse must be float32 [B, H], contiguous")
+    max_pages = page_table.shape[1]
+    a = PrefixAttnArgs(B, H, D, dv, _DTYPES[dtype], _DTYPES[o.dtype], max_pages, int(prefix_len), scale, *_pool(kv_pool, D),
+                       q.data_ptr(), kv_pool.data_ptr(), _ints(page_table, B * max_pages, "page_table"), _ints(lens, B, "lens"),
+                       o.data_ptr(), lse.data_ptr())
     a._refs = (q, kv_pool, page_table, lens, o, lse)
     return a
 
@@ -537,8 +570,13 @@ def ls_prefix_attn_workspace_size(a: PrefixAttnArgs) -> int:
 
 
 def ls_prefix_attn_decode(a: PrefixAttnArgs, workspace=None, stream=None):
+    device = torch.cuda.current_device()
+    if a._device != device:
+        _check_device(a, device)
+    if workspace is not None and workspace.get_device() != device:
+        raise LsError(LS_ERR_INVALID_ARG, "the workspace is not on the current device")
     _check(lib().ls_prefix_attn_decode(C.byref(a), _ptr(workspace), 0 if workspace is None else workspace.numel(),
-                                       _stream(stream)))
+                                       _stream(stream, device)))
 
 
 # ------------------------------------------------------------------------------- a7

@@ -213,3 +213,30 @@ def test_outputs_of_head_rows_as_given():
 def test_queries_and_outputs_of_the_attention_that_are_refused(kw):
     with pytest.raises(B.LsError):
         prefix_call(**kw)
+
+
+# ------------------------------------------------------------------------------- devices
+@pytest.mark.parametrize("call", [heads_call, append_call, prefix_call])
+def test_tensors_that_the_kernel_cannot_reach_are_refused(call):
+    with pytest.raises(B.LsError):
+        B._check_device(call(), 0)  # pageable host memory
+
+
+class Elsewhere:
+    """Stands for a tensor of device `dev`, or of host memory."""
+
+    def __init__(self, dev, pinned=False):
+        self.get_device, self.is_pinned = (lambda: dev), (lambda: pinned)
+
+
+def test_devices_are_looked_at_once_for_each_device():
+    a = prefix_call()
+    a._refs = (Elsewhere(1), None, Elsewhere(-1, True))
+    with pytest.raises(B.LsError):
+        B._check_device(a, 0)
+    B._check_device(a, 1)
+    assert a._device == 1
+    a._refs = (Elsewhere(0),)
+    with pytest.raises(B.LsError):
+        B._check_device(a, 2)
+    B._check_device(B.PrefixAttnArgs(), 0)  # a struct filled in by hand: addresses only

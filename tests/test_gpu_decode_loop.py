@@ -128,3 +128,31 @@ def test_append_to_a_view_and_attend_over_it(view):
     assert torch.equal(whole, want)
     check_attention(dict(q=q, pool=pick(want), table=table), o, lse, scale=SCALE, lens=lens)
     assert B.ls_check_device_status() == 0
+
+
+def test_host_tensors_pinned_or_refused():
+    """Index arrays may lie in pinned host memory; what the GPU cannot reach is refused before any launch."""
+    g = torch.Generator(device=DEV).manual_seed(4)
+    x = torch.randn(5, 2, 128, generator=g, device=DEV)
+    cs = torch.randn(10, 64, generator=g, device=DEV)
+    pos = torch.arange(5, dtype=torch.int32)
+    out, want = torch.zeros_like(x), torch.zeros_like(x)
+    B.ls_qk_norm_rope(pos=pos.to(DEV), cos_sin=cs, q=B.head_rows(x, rope_begin=0), q_out=want)
+    B.ls_qk_norm_rope(pos=pos.pin_memory(), cos_sin=cs, q=B.head_rows(x, rope_begin=0), q_out=out)
+    assert torch.equal(out, want)
+    for kw in (dict(pos=pos), dict(cos_sin=cs.cpu()), dict(q=B.head_rows(x.cpu(), rope_begin=0)), dict(q_out=torch.zeros(5, 2, 128)),
+               dict(q=B.head_rows(x, norm=B.LS_NORM_RMS, weight=torch.ones(128), rope_begin=0))):
+        with pytest.raises(B.LsError):
+            B.ls_qk_norm_rope(**dict(dict(pos=pos.to(DEV), cos_sin=cs, q=B.head_rows(x, rope_begin=0), q_out=out), **kw))
+    d = dict(q=torch.zeros(1, 8, 576, dtype=torch.bfloat16, device=DEV), kv_pool=torch.zeros(9, 64, 576, dtype=torch.bfloat16, device=DEV),
+             page_table=torch.zeros(1, 9, dtype=torch.int32, device=DEV), lens=torch.zeros(1, dtype=torch.int32, device=DEV),
+             o=torch.zeros(1, 8, 512, device=DEV), lse=torch.zeros(1, 8, device=DEV), scale=SCALE)
+    a = B.prefix_attn_args(**d)
+    ws = torch.zeros(max(256, B.ls_prefix_attn_workspace_size(a)), dtype=torch.uint8)
+    with pytest.raises(B.LsError):
+        B.ls_prefix_attn_decode(a, ws)
+    for name in ("q", "kv_pool", "page_table", "lens", "o", "lse"):
+        with pytest.raises(B.LsError):
+            B.ls_prefix_attn_decode(B.prefix_attn_args(**dict(d, **{name: d[name].cpu()})), ws.to(DEV))
+    torch.cuda.synchronize()
+    assert B.ls_check_device_status() == 0
