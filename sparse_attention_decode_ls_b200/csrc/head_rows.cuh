@@ -203,6 +203,12 @@ __device__ __forceinline__ uint32_t e4m3x2(float2 v) {
   return __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
 }
 
+// 448 / m, for m in [1e-12, inf].  (The fast quotient is 0 for divisors above 2^126, which rows without
+// a norm can have: both sides are taken 2^9 times smaller, which changes no other bit.)
+__device__ __forceinline__ float e4m3_inv_scale(float m) {
+  return __fdividef(kE4m3Max * 0x1p-9f, m * 0x1p-9f);
+}
+
 template <int G>
 __device__ __forceinline__ float group_sum(float v, uint32_t mask) {
 #pragma unroll
@@ -387,7 +393,7 @@ __device__ __forceinline__ void head_row(const HeadRows& r, float2 (*v)[VEC / 2]
     m = fmaxf(group_max<G>(m, mask), 1e-12f);
     // codes of v * (448 / max): within 2^-22 of the quotient by the scale, which matters only to
     // values that near a tie of two codes: either is then half a step off
-    const float isc = __fdividef(kE4m3Max, m);
+    const float isc = e4m3_inv_scale(m);
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       const int d = (gl + G * i) * VEC;
@@ -461,7 +467,7 @@ __device__ __forceinline__ void head_row_plain(const HeadRows& r, const T* x, co
     m = fmaxf(m, fabsf(v[i]));
   }
   m = fmaxf(group_max<32>(m, 0xffffffffu), 1e-12f);  // (and every lane has read x: out may be x)
-  const float isc = __fdividef(kE4m3Max, m);
+  const float isc = e4m3_inv_scale(m);
 #pragma unroll
   for (int i = 0; i < NC; ++i) {
     const int d = lane + 32 * i;
