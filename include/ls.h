@@ -492,7 +492,8 @@ ls_status ls_attn_merge(const ls_attn_merge_args* args, ls_stream_t stream);
  * j = u + rope_dim / 2 (LS_ROPE_HALVES), counted from rope_begin.  cos_sin[pos] holds the
  * rope_dim / 2 cosines of a position, then its sines.  The result is stored in the row's own
  * type, or as e4m3 codes of y / scale with scale = max(max_d |y_d|, 1e-12) / 448, the form
- * in which a1 takes queries and keys.  float32 throughout, one rounding at the store.
+ * in which a1 takes queries and keys; a row that holds a NaN has a NaN scale and NaN codes, one
+ * that holds an infinity an infinite scale.  float32 throughout, one rounding at the store.
  * Limits: 1 <= dim <= 1024, rope_dim even; any strides and alignment (16-byte multiples are
  * faster).
  * --------------------------------------------------------------------------- */

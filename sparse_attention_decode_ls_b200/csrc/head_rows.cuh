@@ -203,6 +203,18 @@ __device__ __forceinline__ uint32_t e4m3x2(float2 v) {
   return __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
 }
 
+// Maxima that are NaN if an operand is (fmaxf takes the other one): a row's scale is by its definition.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ float abs_max_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 // 448 / m, for m in [1e-12, inf].  (The fast quotient is 0 for divisors above 2^126, which rows without
 // a norm can have: both sides are taken 2^9 times smaller, which changes no other bit.)
 __device__ __forceinline__ float e4m3_inv_scale(float m) {
@@ -218,7 +230,7 @@ __device__ __forceinline__ float group_sum(float v, uint32_t mask) {
 template <int G>
 __device__ __forceinline__ float group_max(float v, uint32_t mask) {
 #pragma unroll
-  for (int o = G / 2; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(mask, v, o, G));
+  for (int o = G / 2; o; o >>= 1) v = max_nan(v, __shfl_xor_sync(mask, v, o, G));
   return v;
 }
 
@@ -389,8 +401,8 @@ __device__ __forceinline__ void head_row(const HeadRows& r, float2 (*v)[VEC / 2]
 #pragma unroll
     for (int i = 0; i < NC; ++i)
 #pragma unroll
-      for (int e = 0; e < VEC / 2; ++e) m = fmaxf(m, fmaxf(fabsf(v[i][e].x), fabsf(v[i][e].y)));
-    m = fmaxf(group_max<G>(m, mask), 1e-12f);
+      for (int e = 0; e < VEC / 2; ++e) m = abs_max_nan(m, v[i][e].x, v[i][e].y);
+    m = max_nan(group_max<G>(m, mask), 1e-12f);
     // codes of v * (448 / max): within 2^-22 of the quotient by the scale, which matters only to
     // values that near a tie of two codes: either is then half a step off
     const float isc = e4m3_inv_scale(m);
@@ -464,9 +476,9 @@ __device__ __forceinline__ void head_row_plain(const HeadRows& r, const T* x, co
       const float o = normed(first ? d + by : d - by), c = cs[at], sn = cs[half + at];
       v[i] = first ? v[i] * c - o * sn : v[i] * c + o * sn;
     }
-    m = fmaxf(m, fabsf(v[i]));
+    m = max_nan(m, fabsf(v[i]));
   }
-  m = fmaxf(group_max<32>(m, 0xffffffffu), 1e-12f);  // (and every lane has read x: out may be x)
+  m = max_nan(group_max<32>(m, 0xffffffffu), 1e-12f);  // (and every lane has read x: out may be x)
   const float isc = e4m3_inv_scale(m);
 #pragma unroll
   for (int i = 0; i < NC; ++i) {

@@ -51,3 +51,46 @@ def test_append_of_a_huge_key(dt):
                       key=B.head_rows(x), key_pool=key, key_scale=ks)
     y, M = reference(x, None, norm=B.LS_NORM_NONE, norm_dim=128, weight=None, bias=None, begin=None, pairs=False)
     check_rows(torch.stack([key[1, 5], key[0, 6]]), torch.stack([ks[1, 5], ks[0, 6]]), y, M)
+
+
+@pytest.mark.parametrize("layout", ["packed", "odd"])
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("dim", [64, 128, 576, 1024])
+def test_infinite_and_nan_rows(dt, layout, dim):
+    """An infinity: scale inf, its own code NaN (inf / inf), the finite values' zero.  A NaN anywhere: the
+    maximum is NaN, so the scale and all codes are.  Other rows are not touched by either."""
+    g = torch.Generator(device=DEV).manual_seed(dim)
+    x = torch.randn(9, 3, dim, generator=g, device=DEV).to(dt)
+    clean = x.clone()
+    for t, d in enumerate((0, 1, dim // 2, dim - 1)):
+        x[t, 1, d] = float("inf") if t % 2 else -float("inf")
+        x[t + 4, 1, d] = float("nan")
+    out, scale = to_e4m3(x, layout)
+    v = out.view(torch.float8_e4m3fn).float()
+    assert (scale[:4, 1] == float("inf")).all()
+    inf = x[:4, 1].isinf()
+    assert v[:4, 1][inf].isnan().all() and (v[:4, 1][~inf] == 0).all()
+    assert scale[4:8, 1].isnan().all() and v[4:8, 1].isnan().all()
+    want, want_scale = to_e4m3(clean, layout)
+    others = torch.ones(9, 3, dtype=torch.bool, device=DEV)
+    others[:8, 1] = False
+    assert torch.equal(out[others], want[others]) and torch.equal(scale[others], want_scale[others])
+
+
+@pytest.mark.parametrize("norm", [B.LS_NORM_RMS, B.LS_NORM_LAYER])
+@pytest.mark.parametrize("layout", ["packed", "odd"])
+def test_nan_through_a_norm(norm, layout):
+    """The norm carries a NaN to every value of its row: NaN scale and codes, or NaN values."""
+    g = torch.Generator(device=DEV).manual_seed(3)
+    buf = torch.randn(4, 2 * 128 + (3 if layout == "odd" else 0), generator=g, device=DEV).to(torch.bfloat16)
+    x = buf[:, (1 if layout == "odd" else 0):][:, :256].unflatten(1, (2, 128))
+    x[2, 1, 77] = float("nan")
+    pos = torch.zeros(4, dtype=torch.int32, device=DEV)
+    out, scale, same = torch.zeros(4, 2, 128, dtype=torch.uint8, device=DEV), torch.zeros(4, 2, device=DEV), torch.zeros(4, 2, 128, dtype=torch.bfloat16, device=DEV)
+    r = B.head_rows(x, norm=norm)
+    B.ls_qk_norm_rope(pos=pos, q=r, q_out=out, q_scale=scale, k=r, k_out=same)
+    nan = torch.zeros(4, 2, dtype=torch.bool, device=DEV)
+    nan[2, 1] = True
+    assert torch.equal(scale.isnan(), nan)
+    v = out.view(torch.float8_e4m3fn).float()
+    assert torch.equal(v.isnan(), nan[..., None].expand_as(v)) and torch.equal(same.isnan(), nan[..., None].expand_as(same))
