@@ -596,8 +596,10 @@ ls_status ls_cache_append(const ls_cache_append_args* args, ls_stream_t stream);
  * all been written.  They are read through page_table[0] and computed once for the query
  * rows of all requests; the positions behind them (the tail of a prefix that ends inside
  * a page included) through each request's own table.  The result is that of prefix_len = 0
- * up to float32 rounding, at any value, and a length below prefix_len is honoured.
+ * up to float32 rounding, at any value, and a length below prefix_len is honoured (for shared rows
+ * without NaN and infinities: those may also reach a request that ends before them).
  *
+ * A NaN or +inf among a row's scores makes its o and lse NaN; a score of -inf has no weight.
  * Rows behind lens[b] on a request's own pages are not read into the result, whatever they
  * hold (NaN included).  A page id out of range is skipped (its positions are masked) and
  * flagged, a length out of [0, 64 * max_pages] is clamped and flagged.

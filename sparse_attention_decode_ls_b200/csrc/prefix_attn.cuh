@@ -672,7 +672,10 @@ __global__ void __launch_bounds__(pfx::kThreads, 1)
       const float total = (sums[r64] + sums[64 + r64]) + (sums[128 + r64] + sums[192 + r64]);
       __syncwarp();  // (bar.sync and tcgen05.ld are .aligned: the warp has to be whole before them)
       asm volatile("bar.sync 1, 256;" ::: "memory");
-      const float inv = total > 0.f ? 1.f / total : 0.f;
+      // zero: nothing to see (else at least the weight of the maximum, 1).  A NaN or +inf among the scores
+      // makes the sum NaN, and o and lse with it
+      const bool some = total != 0.f;
+      const float inv = 1.f / total;
       const int row = w.row0 + rr;
       if (w.tiles > 0) {
         tc_fence_after();
@@ -691,7 +694,7 @@ __global__ void __launch_bounds__(pfx::kThreads, 1)
           } else if (p.o_f32) {
             float* o = (float*)p.o + (size_t)row * DV + d0;
 #pragma unroll
-            for (int c = 0; c < 64; ++c) v[c] = total > 0.f ? v[c] * inv : 0.f;
+            for (int c = 0; c < 64; ++c) v[c] = some ? v[c] * inv : 0.f;
 #pragma unroll
             for (int c = 0; c < 64; c += 4) *(float4*)(o + c) = make_float4(v[c], v[c + 1], v[c + 2], v[c + 3]);
           } else {
@@ -702,7 +705,7 @@ __global__ void __launch_bounds__(pfx::kThreads, 1)
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
                 __nv_bfloat162 two = __floats2bfloat162_rn(v[c + 2 * k] * inv, v[c + 2 * k + 1] * inv);
-                x[k] = *(uint32_t*)&two;
+                x[k] = some ? *(uint32_t*)&two : 0u;
               }
               o[c / 8] = make_uint4(x[0], x[1], x[2], x[3]);
             }
@@ -720,10 +723,10 @@ __global__ void __launch_bounds__(pfx::kThreads, 1)
       }
       if (live && page == 0) {
         if (p.direct) {
-          p.lse[row] = total > 0.f ? (m_run + log2f(total)) * kLn2 : -INFINITY;
+          p.lse[row] = some ? (m_run + log2f(total)) * kLn2 : -INFINITY;
         } else {
           float2* ml = (float2*)p.part_ml + w.part + rr;
-          *ml = total > 0.f ? make_float2(m_run, total) : make_float2(-INFINITY, 0.f);
+          *ml = some ? make_float2(m_run, total) : make_float2(-INFINITY, 0.f);
         }
       }
       __syncwarp();
@@ -783,7 +786,7 @@ __global__ void __launch_bounds__(256) prefix_attn_combine(const PrefixParams p)
       for (int e = 0; e < 8; ++e) x[j][e] = 0.f;
       if (i0 + j < n) {
         const float2 v = ml_all[(i0 + j) * kCombineRows + lane];
-        if (v.y > 0.f) {  // (a unit without positions has written no values)
+        if (v.y != 0.f) {  // (a unit without positions has written no values)
           long long u0;
           int at, nr;
           part(i0 + j, u0, at, nr);
@@ -799,7 +802,7 @@ __global__ void __launch_bounds__(256) prefix_attn_combine(const PrefixParams p)
       for (int e = 0; e < 8; ++e) acc[e] = fmaf(wgt[j], x[j][e], acc[e]);
   }
   if (row >= rows) return;
-  const float inv = total > 0.f ? 1.f / total : 0.f;
+  const float inv = total != 0.f ? 1.f / total : 0.f;  // (NaN stays NaN)
   if (p.o_f32) {
     float4* o = (float4*)((float*)p.o + (size_t)row * DV + d8 * 8);
     o[0] = make_float4(acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv);
@@ -813,7 +816,7 @@ __global__ void __launch_bounds__(256) prefix_attn_combine(const PrefixParams p)
     }
     *(uint4*)((__nv_bfloat16*)p.o + (size_t)row * DV + d8 * 8) = make_uint4(x[0], x[1], x[2], x[3]);
   }
-  if (d8 == 0) p.lse[row] = total > 0.f ? (M + log2f(total)) * kLn2 : -INFINITY;
+  if (d8 == 0) p.lse[row] = total != 0.f ? (M + log2f(total)) * kLn2 : -INFINITY;
 }
 
 }  // namespace ls
