@@ -390,7 +390,12 @@ def head_rows(x, *, norm=LS_NORM_NONE, norm_dim=None, weight=None, bias=None, ep
     dim = shape[-1]
     if stride[-1] != 1 and dim > 1:
         raise LsError(LS_ERR_INVALID_ARG, "the values of a row must be contiguous")
-    heads, head_stride = (shape[1], stride[1]) if len(shape) == 3 else (1, 0)
+    if len(shape) == 3:
+        heads, head_stride = shape[1], stride[1]
+    elif len(shape) == 2:
+        heads, head_stride = 1, 0
+    else:
+        raise LsError(LS_ERR_INVALID_ARG, "x must be [tokens, heads, dim] or [tokens, dim]")
     n = dim if norm_dim is None else norm_dim
     w_dtype, w, b = LS_BF16, None, None
     if bias is not None:

@@ -41,6 +41,12 @@ def test_weights_as_long_as_the_normalised_part():
         B.head_rows(x, norm=B.LS_NORM_RMS, weight=torch.ones(512))
 
 
+@pytest.mark.parametrize("shape", [(128,), (2, 4, 3, 128)])
+def test_rows_of_another_rank_are_refused(shape):
+    with pytest.raises(B.LsError):
+        B.head_rows(torch.zeros(*shape, dtype=BF))
+
+
 # ------------------------------------------------------------------------------- two operands
 def heads_call(**kw):
     d = dict(pos=torch.zeros(4, dtype=torch.int32), cos_sin=torch.zeros(100, 64), q=B.head_rows(torch.zeros(4, 3, 128, dtype=BF)),
