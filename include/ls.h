@@ -523,7 +523,8 @@ typedef struct ls_head_out {
   int32_t dtype;              /* the rows' dtype, or LS_E4M3 */
   int64_t token_stride;       /* elements; no two rows may overlap */
   int64_t head_stride;
-  void* out;                  /* may be x, with the same strides and dtype */
+  void* out;                  /* may be x, with the same strides and dtype; may not overlap the other
+                                 operand's rows or output */
   float* scale;               /* [tokens, heads] out (LS_E4M3 only, else NULL) */
 } ls_head_out;
 

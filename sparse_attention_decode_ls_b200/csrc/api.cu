@@ -1478,6 +1478,10 @@ ls_status ls_qk_norm_rope(const ls_qk_norm_rope_args* a, ls_stream_t stream) {
                        (a->q.heads > 0 && a->q.rope_begin >= 0) || (a->k.heads > 0 && a->k.rope_begin >= 0)));
   LS_TRY(validate_out(&a->q, &a->q_out, "q", a->tokens, a->dtype));
   LS_TRY(validate_out(&a->k, &a->k_out, "k", a->tokens, a->dtype));
+  // (the two run side by side: what one writes the other may not read or write)
+  LS_REQUIRE(a->q.heads == 0 || a->k.heads == 0 ||
+                 (a->q_out.out != a->k_out.out && a->q_out.out != a->k.x && a->k_out.out != a->q.x),
+             "an output may not be the other operand's rows or output");
   ls::HeadRowsParams p{};
   p.a = to_rows(&a->q);
   p.b = to_rows(&a->k);
@@ -1522,6 +1526,9 @@ ls_status ls_cache_append(const ls_cache_append_args* a, ls_stream_t stream) {
   LS_TRY(validate_out(&a->key, &key_out, "key", 2, a->dtype));
   LS_REQUIRE((a->kv.heads == 0 || a->kv_pool != a->kv.x) && (a->key.heads == 0 || a->key_pool != a->key.x),
              "a pool may not be the new rows themselves");
+  LS_REQUIRE(a->kv.heads == 0 || a->key.heads == 0 ||
+                 (a->kv_pool != a->key_pool && a->kv_pool != a->key.x && a->key_pool != a->kv.x),
+             "a pool may not be the other pool or its new rows");
   ls::HeadRowsParams p{};
   p.a = to_rows(&a->kv);
   p.b = to_rows(&a->key);

@@ -246,3 +246,24 @@ def test_devices_are_looked_at_once_for_each_device():
     with pytest.raises(B.LsError):
         B._check_device(a, 2)
     B._check_device(B.PrefixAttnArgs(), 0)  # a struct filled in by hand: addresses only
+
+
+# ------------------------------------------------------------------------------- operands that share memory
+@pytest.fixture(scope="module")
+def lib():
+    from sparse_attention_decode_ls_b200 import build as build_mod
+    build_mod.build()
+    return B.lib()
+
+
+def test_outputs_over_the_other_operand_are_refused(lib):
+    q, k = torch.zeros(4, 3, 128, dtype=BF), torch.zeros(4, 3, 128, dtype=BF)
+    for q_out, k_out in ((k, torch.zeros_like(k)), (torch.zeros_like(q), q), (k, q), (torch.zeros_like(q),) * 2):
+        a = heads_call(q=B.head_rows(q), k=B.head_rows(k), q_out=q_out, k_out=k_out)
+        assert lib.ls_qk_norm_rope(B.C.byref(a), None) == B.LS_ERR_INVALID_ARG
+        assert "other operand" in lib.ls_get_error_string().decode()
+    x = torch.zeros(5, 128, dtype=BF)
+    pool = torch.zeros(8, 64, 128, dtype=BF)
+    a = append_call(kv=B.head_rows(x), key=B.head_rows(torch.zeros(5, 128, dtype=BF)), kv_pool=pool, key_pool=pool, key_scale=None)
+    assert lib.ls_cache_append(B.C.byref(a), None) == B.LS_ERR_INVALID_ARG
+    assert "other pool" in lib.ls_get_error_string().decode()
