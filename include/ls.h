@@ -494,8 +494,8 @@ ls_status ls_attn_merge(const ls_attn_merge_args* args, ls_stream_t stream);
  * type, or as e4m3 codes of y / scale with scale = max(max_d |y_d|, 1e-12) / 448, the form
  * in which a1 takes queries and keys; a row that holds a NaN has a NaN scale and NaN codes, one
  * that holds an infinity an infinite scale.  float32 throughout, one rounding at the store.
- * Limits: 1 <= dim <= 1024, rope_dim even; any strides and alignment (16-byte multiples are
- * faster).
+ * Limits: 1 <= dim <= 1024, rope_dim even; any strides and alignment (a call is faster, up to 14
+ * times, if dims, strides, addresses and the rotated part of both its operands are 16-byte multiples).
  * --------------------------------------------------------------------------- */
 #define LS_NORM_NONE 0
 #define LS_NORM_RMS 1

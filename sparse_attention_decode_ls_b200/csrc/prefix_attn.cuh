@@ -20,17 +20,24 @@
 //   CTAs makes them either swap S or compute it twice.  With M 128 over the pair and N 256 all
 //   MMAs run at full rate, S is computed once and only row maxima cross lanes.
 //   The price is shared-memory fill: K (half of the tile's rows, 576 dims) and V (all rows,
-//   half of the 512 dims) are loaded separately, 63 bytes per clock and SM at full MMA rate, and
-//   eight 16 KB slots in flight, each held about 2,400 clocks from its load to its reuse, give 50.
-//   A page's P goes to PV as soon as it is written, into a ring of three pages, which left room for
-//   the eighth slot (without the softmax 277 -> 220 us).
+//   half of the 512 dims) are loaded separately, 278,528 bytes per SM and tile: 63 bytes per clock at
+//   full MMA rate.  Eight 16 KB slots in flight, each held about 2,400 clocks from its load to its
+//   reuse, allow 54.6, or 5,100 clocks per tile.  A page's P goes to PV as soon as it is written, into a
+//   ring of three pages, which left room for the eighth slot (without the softmax 277 -> 220 us).
 //   What the issuing thread does between two MMAs (75 clocks for a wait that has already completed,
 //   32 for a commit) leaves the tensor cores idle, so one warp issues S, another PV, and each fills
 //   the other's gaps (two issuers: 64 clocks per MMA, commits and waits included; one: 100).
 // Measured, 8 requests x 128 heads over 131,072 shared positions and up to 1,024 of their own: 284 us,
 // 1,030 TFLOP/s, 0.63 of the measured cuBLAS bf16 burst; back to back for seconds, at the 1,000 W
 // power cap and 1.7 GHz, 323 us (0.65 of cuBLAS under the same cap).  Tensor pipe 51 % active, DRAM
-// 7 %, L2 hit rate 81 %.  What bounds it: the turnaround of the load slots, then power.
+// 7 %, L2 hit rate 81 %.
+// What bounds it: no part alone.  A tile takes 8,400 clocks (at 1.67 GHz): its MMAs need 4,400, the loads without
+// MMAs 4,600 (158 us), loads and MMAs without the softmax 6,400 (220 us: MMAs wait for slots and slots
+// for MMAs).  The other 2,000 are softmax and hand-over of P that nothing hides: PV of a tile waits
+// for its P, and S is ahead by two tiles at most.  For seconds, power.
+// One request of 128 heads (device time of a call): 7.4 us for a length of 0 (launch, set-up and exit of the
+// pair), 12.9 for 1 to 64 (page ids -> Q, K, V -> S -> softmax -> PV -> store), 13.7 for a whole tile of
+// 256, 15.7 for 200: the rows of V on the last page come one request for four rows then.
 #pragma once
 #include "common.cuh"
 
@@ -225,10 +232,10 @@ __device__ __forceinline__ bool softmax_sync_and(bool v) {
 
 // Rank 0 of the pair issues every MMA; the barriers that count loads (full, q_full) live in its
 // shared memory and take both CTAs' bytes, those it signals (empty, q_free, s_full, p_free, pv_done)
-// exist in both.  S runs up to two tiles ahead of PV.  The softmax warps arrive on barriers of their own CTA: an arrival in the other
-// CTA with cluster scope costs each of them about a thousand clocks, so in rank 1 the two warps
-// that have no MMAs to issue pass the news on (305 -> 289 us at 8 x 128 heads, 131,072 positions).  S runs up to two tiles ahead of PV, so that the softmax of a tile has the MMAs of others
-// to hide behind.
+// exist in both.  S runs up to two tiles ahead of PV, so that the softmax of a tile has the MMAs of
+// others to hide behind.  The softmax warps arrive on barriers of their own CTA: an arrival in the
+// other CTA with cluster scope costs each of them about a thousand clocks, so in rank 1 the two warps
+// that have no MMAs to issue pass the news on (305 -> 289 us at 8 x 128 heads, 131,072 positions).
 __global__ void __launch_bounds__(pfx::kThreads, 1)
     attn_prefix_tc(const PrefixParams p, const __grid_constant__ CUtensorMap kv_map,
                    const __grid_constant__ CUtensorMap v_map, const __grid_constant__ CUtensorMap row_map,

@@ -30,7 +30,7 @@ def innermost_loop(text, at):
 def test_aligned_instructions_come_behind_a_point_where_the_warp_is_whole():
     """tcgen05.ld / st and bar.sync are .aligned: all lanes of a warp have to execute them together.  In a
     loop some of whose lanes take a branch of their own (rows that are not live), nothing brings
-    the lanes together again before its next round but a barrier of the warp."""
+    the lanes together again before its next pass but a barrier of the warp."""
     text = code("prefix_attn.cuh")
     seen = 0
     for m in ALIGNED.finditer(text):
